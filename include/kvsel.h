@@ -402,8 +402,10 @@ typedef struct kvsel_kv_src {
  * "NOSA" and "SparDA": kernels that read host memory directly); a block
  * index >= host_blocks latches BOUNDS and is skipped. PAGED_E4M3 and
  * PAGED_INT8: as PAGED on 8-bit pages (kvsel_q8_write); the codes become f16
- * exactly, the softmax weights keep about 22 bits, everything else is fp32, so
- * the result is that of the values the codes stand for. A row that was not
+ * exactly and everything else is fp32 but the weights, so the result is that of
+ * the values the codes stand for: with w a token's softmax weight times its V
+ * row's power of two, w keeps 22 bits down to 2^-17 of the largest w it is summed
+ * with, and below that is off by at most 2^-40 of the largest. A row that was not
  * finite when it was written makes the outputs that attend it NaN.
  * out: device fp32 output; out_bf16: optional bf16 copy; lse: device fp32.
  * ws: kvsel_workspace_size(p, KVSEL_WS_SPARSE_DECODE) bytes (no initial

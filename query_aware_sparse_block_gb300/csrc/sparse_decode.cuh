@@ -65,12 +65,15 @@
 //    channels, so q's fragment takes the same channel order, and V's fragment
 //    pairs channels 2g and 2g + 1 on rows g and g + 8;
 //  * q becomes f16 scaled by a power of two per query head (largest magnitude in
-//    [2^14, 2^15)): exact down to 2^-38 of the head's largest element;
+//    [2^14, 2^15)): exact down to 2^-31 of the head's largest element, smaller ones are
+//    off by at most 2^-39 of it (half the step of f16's subnormal numbers);
 //  * a token's K factor 2^e multiplies its scores in fp32; its V factor 2^v joins
 //    the softmax weight, p' = 2^(x + v - R) with R the running maximum of x + v
 //    kept beside that of x, so p' <= 1 whatever the factors are; the state's
-//    output is brought back by 2^(R - m) when it is stored. p' is split into f16
-//    high and low parts (22 bits).
+//    output is brought back by 2^(R - m) when it is stored. p' 2^15 is split into f16
+//    high and low parts: 22 bits down to p' = 2^-17, below that off by at most 2^-40.
+//    (f16 ends at 2^-24: unscaled, a token of p' = 2^-20 beside a peak keeps five bits
+//    and one below 2^-25 none, yet both count in the sum.)
 #pragma once
 
 #include <climits>
@@ -122,6 +125,9 @@ constexpr int kDenseSeq = 1 << 30;     // flag beside a sequence's length (at mo
 constexpr int kFirstJoined = 1 << 30, kLastJoined = 1 << 29;
 constexpr int kMinTilesPerCta = 4;
 constexpr int kMaxStages = 8;
+// 8-bit pages: the softmax weights, at most 1, times this are the f16 operands. Scaling by a
+// power of two is exact; 2^15 is the largest that f16 holds.
+constexpr float kWeightScale = 0x1p15f;
 
 // Blocks of a tile: a warp of the 8-bit kernel takes 32 tokens, so blocks of 16
 // come in pairs (the 2 o-th and the next of the attended ones, two copies).
@@ -222,7 +228,7 @@ __device__ __forceinline__ uint32_t swz8(uint32_t stage, int h, int kv, int row,
 // One warp's TS subtiles of 16 token rows of one head of an 8-bit tile (subtile
 // s at st + s * step, rows from r0 + s * 16 % B, cnt[s] of them valid): the running maxima
 // of x (mh) and of x + v (rh), the sum of 2^(x - mh) and the output in units of
-// 2^rh, for the query heads in qb (f16, scaled back by qs).
+// 2^rh / kWeightScale, for the query heads in qb (f16, scaled back by qs).
 template <int D, int B, int NTH, int FMT, int TS>
 __device__ __forceinline__ void q8_tile(uint32_t st0, uint32_t step, int h, int row0, const int (&cnt)[TS],
                                         const uint32_t (&qb)[D / 16][NTH][2],
@@ -336,7 +342,7 @@ __device__ __forceinline__ void q8_tile(uint32_t st0, uint32_t step, int h, int 
         const float m = mh[n][e & 1], r = rh[n][e & 1];
         lh[n][e & 1] += ex2(x[s][n][e] - (m == -INFINITY ? 0.f : m));
         const float y = x[s][n][e] + vx[s][e >> 1] - (r == -INFINITY ? 0.f : r);
-        pv[e] = 8 * (e >> 1) + gq < cnt[s] ? ex2(y) : 0.f;
+        pv[e] = 8 * (e >> 1) + gq < cnt[s] ? ex2(y) * kWeightScale : 0.f;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -916,11 +922,13 @@ __global__ void __launch_bounds__(RINGS * (4 / TS) * 32, 1) sparse_decode_kernel
               dst[1] = lh[n][c];
             }
             if constexpr (kQ8) {
+              // two factors: V's exponent may be as low as -124, their product then underflows
               const float back = rh[n][c] == -INFINITY ? 1.f : ex2(rh[n][c] - (mh[n][c] == -INFINITY ? 0.f : mh[n][c]));
+              constexpr float kUnscale = 1.f / kWeightScale;
 #pragma unroll
               for (int mt = 0; mt < kMT; ++mt)
                 *reinterpret_cast<float2*>(dst + 4 + mt * 16 + 2 * gq) =
-                    make_float2(o[mt][n][c] * back, o[mt][n][c + 2] * back);
+                    make_float2(o[mt][n][c] * kUnscale * back, o[mt][n][c + 2] * kUnscale * back);
               continue;
             }
 #pragma unroll

@@ -1,0 +1,83 @@
+"""GPU: the 8-bit KV pages where the arithmetic's range and order show: tails of
+small weights beside peaks, sums that round, strided rows of a bound layer."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _q8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def K():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from query_aware_sparse_block_gb300.build import build_library
+    build_library()
+    from query_aware_sparse_block_gb300 import kvsel
+    kvsel.lib()
+    torch.cuda.set_device(0)
+    return kvsel
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error(K):
+    K.kvsel_get_error()
+    yield
+    assert K.kvsel_get_error() == 0, "a kernel latched a device error"
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("hq", [4, 12])
+@pytest.mark.parametrize("fmt,d,B", [("e4m3", 128, 32), ("int8", 64, 16), ("e4m3", 64, 64)])
+@pytest.mark.parametrize("peak", ["weight", "value"])
+def test_a_tail_beside_peaks_keeps_its_part_of_every_channel(K, peak, fmt, d, B, hq):
+    """4096 tokens, every 16th a peak whose V row is 0 but in channel 0: the other channels are the tail's alone, whose
+    weights (peak "weight"), or weights against the peaks' V factors (peak "value"), are 2^-22 to 2^-30 of the peaks'."""
+    from query_aware_sparse_block_gb300.runtime import Q8Cache, SparseDecoder
+    T, mb = 4096, 4096 // B
+    dec = SparseDecoder(1, hq, 1, d, B, mb, device="cuda:0")
+    g = torch.Generator().manual_seed(d + B + hq)
+    cache = Q8Cache(dec, fmt, torch.randperm(mb, generator=g).view(1, mb).to(torch.int32).cuda(), n_pages=mb)
+    top = torch.zeros(T, dtype=torch.bool)
+    top[::16] = True
+    fall = 22 + 8 * torch.rand(T, generator=g)                           # log2 of a peak over the token
+    k, v = torch.zeros((T, 1, d)), torch.randn((T, 1, d), generator=g).abs()
+    v[top] = 0
+    v[top, 0, 0] = 1.0
+    if peak == "weight":
+        k[:, 0, 0] = torch.where(top, 0.0, -fall * float(np.log(2)) / 4)  # the score is 4 k_0
+    else:
+        v *= torch.where(top, 1.0, 2.0 ** -fall)[:, None, None]
+    q = torch.zeros((1, hq, d))
+    q[..., 0] = 4 / dec.scale
+    k, v, q = (x.to(torch.bfloat16).cuda() for x in (k, v, q))
+    cache.write(_i32([0, T]), _i32([0]), k, v)
+    dec.n_sel[0] = mb
+    dec.sel_idx[0] = torch.arange(mb, dtype=torch.int32)
+    dec.attend(q, cache.kv, _i32([T]))
+    torch.cuda.synchronize()
+    x = _q8.values(cache.pages.cpu().numpy(), B, d, fmt)
+    ks, vs = (np.concatenate([x[n, 0, w] for n in cache.block_table[0].tolist()]) for w in (0, 1))
+    qd = q[0].double().cpu().numpy()
+    ref, z, reach = _q8.attend(qd, ks, vs, dec.scale)
+    p = np.exp(qd @ ks.T * dec.scale - z[:, None])                       # [hq][T]
+    # A channel's sum is off by the relative error of a weight and of the sums (as _q8.tolerances counts them, the
+    # weight's own rounding 2^-22 of it), and by the weights' smallest step: 2^-40 of the largest weight times V
+    # factor in a state, times a code. A row's largest code is at least half the format's largest (e4m3: 224 of 448;
+    # int8: 64 of 127), so step times code is at most 2^-40 * 2 of the largest weight times value.
+    w = (d + 4) * 2.0 ** -23 * reach + 2.0 ** -22
+    rel = 2 * w + 2 * (T / 16 + 32) * 2.0 ** -23 + 2.0 ** -22
+    step = T * 2.0 ** -39 * (p * np.abs(vs).max(-1)).max(-1)
+    bound = (p @ np.abs(vs)) * rel[:, None] + step[:, None]
+    got = dec.out[0].double().cpu().numpy()
+    # the bound tells the tail from nothing: every channel but the peaks' is far above it
+    assert (np.median(np.abs(ref[:, 1:]), axis=1) > 100 * np.median(bound[:, 1:], axis=1)).all()
+    assert (np.abs(got - ref) <= bound).all(), (np.abs(got - ref) / bound).max()
+    assert (np.abs(dec.lse[0].double().cpu().numpy() - z) <= rel + 2.0 ** -23 * np.abs(z)).all()
