@@ -34,8 +34,11 @@
 //  * P is split into bf16 high and low parts (about 16 bits, as in the sparse
 //    decode): O's product takes two passes and keeps fp32-grade outputs; a
 //    single bf16 P would be off by 2^-9 a weight.
-//  * Every wait is bounded; one that runs out latches KVSEL_ERR_TIMEOUT, the
-//    CTA drains its copies and MMAs, frees its tensor memory and returns.
+//  * Every wait on a barrier is bounded; one that runs out latches
+//    KVSEL_ERR_TIMEOUT, the CTA drains its copies and MMAs, frees its tensor
+//    memory and returns. The tensor memory itself is taken when the stream's
+//    earlier kernels are done; a kernel of another stream that shares the SM and
+//    holds columns is waited for.
 //
 // Measured: 64 sequences x 32 heads (2 KV heads, d = 128) behind 131072 tokens,
 // 124 us: 1.11 PFLOP/s of the formula's products, 1.66 with P's two passes (0.84
@@ -256,11 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixArgs a) {
       *dead = 0;
       fence_barrier_init();
     }
-  } else if (warp == 2) {
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Not before the wait: the allocation has no time limit, and while this grid holds an SM's
+  // columns, a kernel before it in the stream that still needs some could never end.
+  if (warp == 2) {
     tmem_alloc(tmem_s, 512);
     tmem_relinquish();
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0) {
     // the prefixes' tiles: prefix sum, and whether all segments are alike
@@ -906,8 +912,8 @@ cudaError_t launch_t(PrefixArgs a, cudaStream_t s) {
   a.v_stages = std::min(kMaxV, tiles - a.k_stages);
   a.unit_rows = ROWS ? 256 : 128;
   const int grid = std::min(kMaxGrid, sm_count());
-  // more than half of an SM's shared memory: CTAs of two such kernels never share
-  // an SM, so the tensor-memory allocation never waits
+  // more than half of an SM's shared memory: CTAs of two such kernels (calls on two
+  // streams) never share an SM, so neither's allocation of tensor memory waits for the other's
   const size_t smem = std::max(rest + (kQTiles + size_t(a.k_stages) + a.v_stages) * op, size_t(120) * 1024);
   auto fn = prefix_kernel<D, ROWS>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(fn), int(smem));
