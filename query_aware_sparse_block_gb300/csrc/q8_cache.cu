@@ -202,13 +202,15 @@ __global__ void __launch_bounds__(kWarps * 32) q8_write_kernel(Q8RowsArgs a) {
   uint8_t* scales = head + 2 * a.B * D;
   const kvsel_bf16* ks = a.k + it.row * a.k_stride + int64_t(h) * D + chunk * 16;
   const kvsel_bf16* vs = a.v + it.row * a.v_stride + int64_t(h) * D + chunk * 16;
-  const int rows = it.t1 - it.t0;
+  // Row t of the block always falls to lane group t % RPW, whichever call writes it: a
+  // summary's sum then has one order, however its block was split into calls.
+  const int rows = it.t1 - it.t0, skip = it.t0 % RPW;   // row r of the call: slot r + skip
   Row16 kv[kUnroll], vv[kUnroll];
   auto load = [&](int r0) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int r = r0 + u * RPW + sub;
-      if (r < rows) {
+      if (r >= 0 && r < rows) {
         kv[u] = load_row16(ks + r * a.k_stride, a.wide);
         vv[u] = load_row16(vs + r * a.v_stride, a.wide);
       } else {
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kWarps * 32) q8_write_kernel(Q8RowsArgs a) {
       }
     }
   };
-  load(0);
+  load(-skip);
   float2 s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = make_float2(0.f, 0.f);
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32) q8_write_kernel(Q8RowsArgs a) {
         if (t0 + u * RPW + sub < it.t0) add_key<FMT>(s, c[u], b[u]);
     }
   }
-  for (int r0 = 0; r0 < rows; r0 += RPW * kUnroll) {
+  for (int r0 = -skip; r0 < rows; r0 += RPW * kUnroll) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (r0 + u * RPW >= rows) break;
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32) q8_write_kernel(Q8RowsArgs a) {
       scale_bytes<FMT, LPR>(kv[u], vv[u], kb, vb);
       const uint4 kc = quantise<FMT>(kv[u], kb);
       const uint4 vc = quantise<FMT>(vv[u], vb);
-      if (r < rows) {
+      if (r >= 0 && r < rows) {
         const int t = it.t0 + r;
         uint8_t* dst = head + q8_chunk_off<D>(t, chunk);
         *reinterpret_cast<uint4*>(dst) = kc;

@@ -81,3 +81,37 @@ def test_a_tail_beside_peaks_keeps_its_part_of_every_channel(K, peak, fmt, d, B,
     assert (np.median(np.abs(ref[:, 1:]), axis=1) > 100 * np.median(bound[:, 1:], axis=1)).all()
     assert (np.abs(got - ref) <= bound).all(), (np.abs(got - ref) / bound).max()
     assert (np.abs(dec.lse[0].double().cpu().numpy() - z) <= rel + 2.0 ** -23 * np.abs(z)).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,B", [(64, 16), (64, 64), (128, 32)])
+def test_summaries_do_not_depend_on_how_a_block_was_split_into_calls(K, fmt, d, B):
+    """Keys of very different sizes, the large ones in pairs that cancel, so that the fp32 sum is inexact and its order
+    shows: a block written at once, in odd chunks and a row at a time."""
+    from query_aware_sparse_block_gb300.runtime import Q8Cache, SparseDecoder
+    batch, H, mb = 2, 2, 3
+    T = mb * B
+    dec = SparseDecoder(batch, H, H, d, B, mb, device="cuda:0")
+    table = torch.arange(batch * mb, dtype=torch.int32).view(batch, mb).cuda()
+    g = torch.Generator().manual_seed(d + B)
+    k = torch.randn((batch, T, H, d), generator=g)
+    k *= 2.0 ** torch.randint(0, 25, (batch, T, 1, 1), generator=g)
+    order = torch.stack([n * B + torch.randperm(B, generator=g) for n in range(mb)]).view(-1)
+    k[:, order[1::2]] = -k[:, order[::2]] * (1 + 2.0 ** -6)               # nearly: its code is another one at times
+    k = k.to(torch.bfloat16).cuda()
+    got = []
+    for sizes in ([T], [7, B, 1, 2 * B], [5, 3, 11], [1]):
+        cache = Q8Cache(dec, fmt, table, n_pages=batch * mb)
+        summ = torch.zeros((batch, mb, H, d), dtype=torch.bfloat16, device="cuda")
+        at, i = 0, 0
+        while at < T:
+            n = min(sizes[i % len(sizes)], T - at)
+            x = k[:, at:at + n].reshape(batch * n, H, d)
+            cache.write(_i32([0, n, 2 * n]), _i32([at, at]), x, x, summ)
+            at, i = at + n, i + 1
+        torch.cuda.synchronize()
+        got.append((cache.pages, summ))
+    assert torch.isfinite(got[0][1]).all() and (got[0][1] != 0).any()
+    for pages, summ in got[1:]:
+        assert torch.equal(pages, got[0][0])
+        assert torch.equal(summ, got[0][1])
