@@ -479,9 +479,12 @@ KVSEL_API size_t kvsel_q8_page_bytes(const kvsel_problem* p);
  * k_stride, v_stride >= n_kvheads * head_dim and multiples of 8 (K and V may be
  * slices of one projection's rows). row_start: device int32 [batch + 1], not
  * decreasing, last entry <= n_rows. start_pos: device int32 [batch].
- * Errors: INVALID_ARG, UNSUPPORTED, CUDA; device BOUNDS for row_start out of
- * order or range (that sequence is skipped), positions past max_blocks *
- * block_size or a block-table entry out of range (those rows are skipped).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA; device BOUNDS for a sequence's rows
+ * outside [0, n_rows] (it is skipped), positions past max_blocks * block_size
+ * or a block-table entry out of range (those rows are skipped), and a row_start
+ * that decreases: that sequence is skipped, and rows of any other sequence may
+ * be left out too, because the work is laid out by row_start. Rows that are
+ * handled are right all the same, and nothing else is touched.
  * Two sequences must not write the same block of a shared page in one call.
  */
 KVSEL_API int kvsel_q8_write(const kvsel_problem* p, const kvsel_q8_cache* cache,
@@ -494,7 +497,8 @@ KVSEL_API int kvsel_q8_write(const kvsel_problem* p, const kvsel_q8_cache* cache
  * and v receives the position that kvsel_q8_write with the same row_start and
  * start_pos would store it at. Rows of skipped sequences and blocks, before
  * row_start[0] and from row_start[batch] on are left as they were. Arguments
- * and errors as kvsel_q8_write.
+ * and errors as kvsel_q8_write; a row that two sequences claim (row_start
+ * decreases) is not specified.
  */
 KVSEL_API int kvsel_q8_read(const kvsel_problem* p, const kvsel_q8_cache* cache,
                             const int32_t* row_start, const int32_t* start_pos, kvsel_bf16* k,

@@ -10,6 +10,8 @@
 // touches at most L / B + 2 blocks and f grows by at least that, so no two
 // sequences share an item; a warp tries sequence i / 2 (right when sequences
 // have few rows, as in a decode step) and else searches f 32 ways at a time.
+// (Where row_start decreases f does too: an item that two sequences then claim
+// goes to one of them, and the other's rows of that block are left out.)
 // One warp per (item, KV head): it owns every row it writes and the block's
 // summary, so nothing needs an atomic or a second pass. A lane holds 16
 // channels: one 32-byte access of bf16 against one 16-byte chunk of codes.

@@ -115,3 +115,45 @@ def test_summaries_do_not_depend_on_how_a_block_was_split_into_calls(K, fmt, d, 
     for pages, summ in got[1:]:
         assert torch.equal(pages, got[0][0])
         assert torch.equal(summ, got[0][1])
+
+
+@pytest.mark.parametrize("start,first", [([0, 100, 50, 60], [15, 0, 0]), ([0, 40, 20, 90], [3, 0, 9]),
+                                         ([90, 100, 0, 80], [0, 1, 16])])
+def test_a_row_start_that_decreases_between_good_sequences(K, start, first):
+    """Latched; rows of the good sequences may be left out, but a handled row is right and nothing else is touched."""
+    from query_aware_sparse_block_gb300.runtime import Q8Cache, SparseDecoder
+    batch, B, d, H, mb, fmt = 3, 16, 64, 2, 8, "e4m3"
+    dec = SparseDecoder(batch, H, H, d, B, mb, device="cuda:0")
+    table = torch.arange(batch * mb, dtype=torch.int32).view(batch, mb)
+    cache = Q8Cache(dec, fmt, table.cuda(), n_pages=batch * mb + 2)
+    g = torch.Generator().manual_seed(3)
+    cache.pages.copy_(torch.randint(0, 120, cache.pages.shape, generator=g, dtype=torch.uint8))
+    before = cache.pages.cpu().numpy()
+    k, v = _q8.rows(g, (100, H, d)).cuda(), _q8.rows(g, (100, H, d)).cuda()
+    good = [b for b in range(batch) if start[b + 1] >= start[b]]
+    want = before.copy()
+    for b in good:
+        one, _ = _q8.write(before, table[b:b + 1].numpy(), [start[b], start[b + 1]], first[b:b + 1],
+                           k.double().cpu().numpy(), v.double().cpu().numpy(), B, fmt, mb)
+        mine = table[b].numpy()
+        want[mine] = one[mine]
+    cache.write(_i32(start), _i32(first), k, v)
+    assert K.kvsel_get_error() == K.KVSEL_ERR_BOUNDS
+    got = cache.pages.cpu().numpy()
+    gc, gs = _q8.split(got, B, d)                                        # a row's codes and its scale byte
+    wc, ws = _q8.split(want, B, d)
+    bc, bs = _q8.split(before, B, d)
+    new = ((gc == wc).all(-1) & (gs == ws))
+    old = ((gc == bc).all(-1) & (gs == bs))
+    assert (new | old).all()
+    # read back: a row is what the page holds, or as it was
+    kb, vb = (torch.full_like(k, 3.0) for _ in range(2))
+    cache.read(_i32(start), _i32(first), kb, vb)
+    assert K.kvsel_get_error() == K.KVSEL_ERR_BOUNDS
+    x = _q8.values(got, B, d, fmt)
+    for r in range(100):
+        at = [(b, first[b] + r - start[b]) for b in good if start[b] <= r < start[b + 1]]
+        for which, y in enumerate((kb, vb)) if len(at) < 2 else ():      # a row that two sequences claim is theirs in parts
+            row = y[r].double().cpu().numpy()
+            may = [x[table[b, pos // B], :, which, pos % B] for b, pos in at]
+            assert (row == 3).all() or any(np.array_equal(row, m) for m in may), r
