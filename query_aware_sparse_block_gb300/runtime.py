@@ -115,7 +115,10 @@ class BoundLayer:
         keeps the layer's K and V in 8 bits: append() is kvsel_q8_write,
         append_select() that and the selection, attend() reads the 8-bit
         pages; kv_pages, block_table and open_acc are then not used and may be
-        None."""
+        None, and new_k and new_v may be slices of a projection's rows
+        ([batch, n_kvheads, head_dim], each row contiguous). Pointers given to
+        append() and append_select() are to rows that lie as new_k's and
+        new_v's do (contiguous ones where the layer has none)."""
         L = K.lib()
         vp = ctypes.c_void_p
         self._fa, self._fs, self._fd = L.kvsel_build_summaries, L.kvsel_score_topk, L.kvsel_sparse_decode
@@ -130,7 +133,8 @@ class BoundLayer:
             self._fq = L.kvsel_q8_write
             self.q8_ref = ctypes.byref(q8.desc)
             self._rows = torch.arange(dec.p.batch + 1, dtype=torch.int32, device=dec.device)   # one row a sequence
-            self.rows, self.row = vp(self._rows.data_ptr()), dec.p.n_kvheads * dec.p.head_dim
+            self.rows = vp(self._rows.data_ptr())
+            self.k_stride, self.v_stride = (self._stride(t, n) for t, n in ((new_k, "new_k"), (new_v, "new_v")))
             kv = kv if kv is not None else q8.kv
         self.kv = kv if kv is not None else K.kv_paged(kv_pages, block_table)
         self.kv_ref = ctypes.byref(self.kv)
@@ -157,12 +161,20 @@ class BoundLayer:
         self._app.summaries, self._app.open_acc = self.summ.value, self.acc.value
         self._app_ref = ctypes.byref(self._app)
 
+    def _stride(self, rows, name):
+        if rows is None:
+            return self.dec.p.n_kvheads * self.dec.p.head_dim
+        n, stride = K._rows(rows, self.dec.p, name)
+        if n != self.dec.p.batch:
+            raise ValueError(f"{name}: expected a row for each of {self.dec.p.batch} sequences, got {n}")
+        return stride
+
     def append(self, append_pos_ptr, stream_ptr, new_k_ptr=None, new_v_ptr=None):
         nk = new_k_ptr if new_k_ptr is not None else self.new_k
         nv = new_v_ptr if new_v_ptr is not None else self.new_v
         if self.q8 is not None:
-            rc = self._fq(self.p, self.q8_ref, self.rows, append_pos_ptr, nk, nv, self.dec.p.batch, self.row,
-                          self.row, self.summ, stream_ptr)
+            rc = self._fq(self.p, self.q8_ref, self.rows, append_pos_ptr, nk, nv, self.dec.p.batch, self.k_stride,
+                          self.v_stride, self.summ, stream_ptr)
             if rc:
                 K._check(rc, "kvsel_q8_write")
             return

@@ -1,0 +1,46 @@
+"""CPU: what BoundLayer takes and refuses for a layer on 8-bit pages (no kernel runs here)."""
+from __future__ import annotations
+
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def K():
+    from query_aware_sparse_block_gb300.build import build_library
+    build_library()
+    from query_aware_sparse_block_gb300 import kvsel
+    kvsel.lib()
+    return kvsel
+
+
+def _layer(K, batch=3, hkv=2, d=64, cache_of=None, **kw):
+    from query_aware_sparse_block_gb300.runtime import BoundLayer, SparseDecoder
+    dec = SparseDecoder(batch, 4, hkv, d, 16, 8, device="cpu")
+    desc = K.kvsel_q8_cache(K.KVSEL_KV_PAGED_E4M3, 16, 4, 16)
+    q8 = SimpleNamespace(p=dec.p if cache_of is None else K.problem(*cache_of), desc=desc, kv=K.kv_paged_q8(desc))
+    t = torch.zeros(1, dtype=torch.bfloat16)
+    return BoundLayer(dec, t, None, None, t, None, dec.out, dec.lse, q8=q8, **kw)
+
+
+def test_rows_of_a_projection_keep_their_strides(K):
+    qkv = torch.zeros((3, 8, 64), dtype=torch.bfloat16)
+    layer = _layer(K, new_k=qkv[:, 4:6], new_v=torch.zeros((3, 2, 64), dtype=torch.bfloat16))
+    assert (layer.k_stride, layer.v_stride) == (512, 128)
+    layer = _layer(K)
+    assert (layer.k_stride, layer.v_stride) == (128, 128)
+
+
+@pytest.mark.parametrize("bad,error", [
+    (torch.zeros((3, 2, 64)), TypeError),
+    (torch.zeros((2, 2, 64), dtype=torch.bfloat16), ValueError),
+    (torch.zeros((3, 128), dtype=torch.bfloat16), ValueError),
+    (torch.zeros((3, 2, 128), dtype=torch.bfloat16)[..., ::2], ValueError),
+    (torch.zeros((2, 3, 64), dtype=torch.bfloat16).transpose(0, 1), ValueError),
+], ids=["fp32", "two rows", "flat", "every second channel", "heads apart"])
+@pytest.mark.parametrize("which", ["new_k", "new_v"])
+def test_rows_that_cannot_be_read_are_refused(K, which, bad, error):
+    with pytest.raises(error, match=which):
+        _layer(K, **{which: bad})

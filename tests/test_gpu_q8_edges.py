@@ -157,3 +157,30 @@ def test_a_row_start_that_decreases_between_good_sequences(K, start, first):
             row = y[r].double().cpu().numpy()
             may = [x[table[b, pos // B], :, which, pos % B] for b, pos in at]
             assert (row == 3).all() or any(np.array_equal(row, m) for m in may), r
+
+
+def test_bound_layer_appends_rows_of_a_projection(K):
+    """new_k and new_v as slices of one projection's rows, of different strides, and a step's own pointers."""
+    import ctypes
+    from query_aware_sparse_block_gb300.runtime import BoundLayer, Q8Cache, SparseDecoder
+    batch, hq, hkv, d, B, mb = 3, 4, 2, 64, 16, 4
+    dec = SparseDecoder(batch, hq, hkv, d, B, mb, device="cuda:0")
+    table = torch.arange(batch * mb, dtype=torch.int32).view(batch, mb).cuda()
+    g = torch.Generator().manual_seed(8)
+    qkv, other = (_q8.rows(g, (batch, hq + 2 * hkv, d)).cuda() for _ in range(2))
+    v = _q8.rows(g, (batch, hkv, d)).cuda()
+    pos, one = _i32([5, 17, 0]), _i32(range(batch + 1))
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def fresh():
+        return Q8Cache(dec, "int8", table, n_pages=batch * mb), torch.zeros((batch, mb, hkv, d), dtype=torch.bfloat16,
+                                                                            device="cuda")
+    for k, given in ((qkv[:, hq:hq + hkv], None), (qkv[:, hq:hq + hkv], other[:, hq:hq + hkv])):
+        want, ws = fresh()
+        want.write(one, pos, (k if given is None else given).contiguous(), v, ws)
+        cache, summ = fresh()
+        layer = BoundLayer(dec, qkv, None, None, summ, None, dec.out, dec.lse, new_k=k, new_v=v, q8=cache)
+        layer.append(ptr(pos), s, None if given is None else ptr(given))
+        torch.cuda.synchronize()
+        assert (cache.pages != 0).any() and torch.equal(cache.pages, want.pages) and torch.equal(summ, ws)
