@@ -44,3 +44,16 @@ def test_rows_of_a_projection_keep_their_strides(K):
 def test_rows_that_cannot_be_read_are_refused(K, which, bad, error):
     with pytest.raises(error, match=which):
         _layer(K, **{which: bad})
+
+
+@pytest.mark.parametrize("field,cache_of", [("batch", (2, 4, 2, 64, 16, 8)), ("n_kvheads", (3, 4, 4, 64, 16, 8)),
+                                            ("head_dim", (3, 4, 2, 128, 16, 8)), ("block_size", (3, 4, 2, 64, 32, 8)),
+                                            ("max_blocks", (3, 4, 2, 64, 16, 4))])
+def test_a_cache_of_another_shape_is_refused(K, field, cache_of):
+    """Its pages or its table would be read and written out of range."""
+    with pytest.raises(ValueError, match=field):
+        _layer(K, cache_of=cache_of)
+
+
+def test_a_cache_of_other_query_heads_is_none_of_another_shape(K):
+    _layer(K, cache_of=(3, 16, 2, 64, 16, 8))
