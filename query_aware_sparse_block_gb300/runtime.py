@@ -131,8 +131,9 @@ class BoundLayer:
         self.q8 = q8
         if q8 is not None:
             for f in ("batch", "n_kvheads", "head_dim", "block_size", "max_blocks"):   # the pages' and the table's shape
-                if getattr(q8.p, f) != getattr(dec.p, f):
-                    raise ValueError(f"q8: a cache of {f} {getattr(q8.p, f)}, the layer has {getattr(dec.p, f)}")
+                has, need = getattr(q8.p, f), getattr(dec.p, f)
+                if has < need if f == "batch" else has != need:                        # more sequences do no harm
+                    raise ValueError(f"q8: a cache of {f} {has}, the layer has {need}")
             self._fq = L.kvsel_q8_write
             self.q8_ref = ctypes.byref(q8.desc)
             self._rows = torch.arange(dec.p.batch + 1, dtype=torch.int32, device=dec.device)   # one row a sequence

@@ -55,5 +55,6 @@ def test_a_cache_of_another_shape_is_refused(K, field, cache_of):
         _layer(K, cache_of=cache_of)
 
 
-def test_a_cache_of_other_query_heads_is_none_of_another_shape(K):
-    _layer(K, cache_of=(3, 16, 2, 64, 16, 8))
+@pytest.mark.parametrize("cache_of", [(3, 16, 2, 64, 16, 8), (7, 4, 2, 64, 16, 8)], ids=["query heads", "more sequences"])
+def test_a_cache_that_the_layer_stays_inside_is_taken(K, cache_of):
+    _layer(K, cache_of=cache_of)
