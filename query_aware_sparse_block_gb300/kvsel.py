@@ -489,7 +489,7 @@ def q8_cache(fmt, pages, block_table) -> kvsel_q8_cache:
     ``fmt`` is KVSEL_KV_PAGED_E4M3 or KVSEL_KV_PAGED_INT8. The tensors stay owned by the caller."""
     _expect(pages, torch.uint8, "pages")
     _expect(block_table, torch.int32, "block_table")
-    return kvsel_q8_cache(int(fmt), _ptr(pages), pages.shape[0], _ptr(block_table))
+    return _placed(kvsel_q8_cache(int(fmt), _ptr(pages), pages.shape[0], _ptr(block_table)), pages, block_table)
 
 
 def kv_paged_q8(cache: kvsel_q8_cache) -> kvsel_kv_src:
@@ -497,7 +497,18 @@ def kv_paged_q8(cache: kvsel_q8_cache) -> kvsel_kv_src:
     s = kvsel_kv_src()
     s.kind = cache.format
     s.kv_pages, s.block_table, s.n_pages = cache.pages, cache.block_table, cache.n_pages
+    if hasattr(cache, "device"):
+        s.device = cache.device
     return s
+
+
+def _placed(desc, *tensors):
+    """Notes the device of a descriptor's tensors, which it holds as pointers only, for _here."""
+    devices = {t.get_device() for t in tensors}
+    if len(devices) > 1:
+        raise ValueError(f"expected tensors on one device, got cuda:{sorted(devices)}")
+    desc.device = devices.pop()
+    return desc
 
 
 def _rows(t, p, name):
@@ -513,14 +524,16 @@ def _rows(t, p, name):
     return n, stride[0] if n > 1 else heads * d
 
 
-def _here(*tensors):
-    """The launch goes to the current device's stream: its tensors have to be there."""
+def _here(*tensors, desc=None):
+    """The launch goes to the current device's stream: its tensors, and those of a descriptor, have to be there."""
     device = torch.cuda.current_device() if tensors[0].is_cuda else None
     for t in tensors:
         if t is not None and t.get_device() != device:
             if not t.is_cuda:
                 raise TypeError("expected CUDA tensors")
             raise ValueError(f"expected tensors on the current device, cuda:{device}, got one on {t.device}")
+    if getattr(desc, "device", device) != device:
+        raise ValueError(f"expected pages and tables on the current device, cuda:{device}, they are on cuda:{desc.device}")
 
 
 def _ragged(p, row_start, start_pos):
@@ -541,7 +554,7 @@ def kvsel_q8_write(p, cache: kvsel_q8_cache, row_start, start_pos, k, v, summari
         _expect(summaries, torch.bfloat16, "summaries", cuda=False)
         if summaries.numel() != p.batch * p.max_blocks * p.n_kvheads * p.head_dim:
             raise ValueError("summaries: expected [batch, max_blocks, n_kvheads, head_dim]")
-    _here(row_start, start_pos, k, v, summaries)
+    _here(row_start, start_pos, k, v, summaries, desc=cache)
     rc = lib().kvsel_q8_write(ctypes.byref(p), ctypes.byref(cache), row_start.data_ptr(), start_pos.data_ptr(),
                               k.data_ptr(), v.data_ptr(), n, ks, vs, _ptr(summaries), _stream(stream))
     if rc:
@@ -554,7 +567,7 @@ def kvsel_q8_read(p, cache: kvsel_q8_cache, row_start, start_pos, k, v, stream=N
     (n, ks), (nv, vs) = _rows(k, p, "k"), _rows(v, p, "v")
     if n != nv:
         raise ValueError("k and v: expected the same number of rows")
-    _here(row_start, start_pos, k, v)
+    _here(row_start, start_pos, k, v, desc=cache)
     rc = lib().kvsel_q8_read(ctypes.byref(p), ctypes.byref(cache), row_start.data_ptr(), start_pos.data_ptr(),
                              k.data_ptr(), v.data_ptr(), n, ks, vs, _stream(stream))
     if rc:
@@ -570,8 +583,9 @@ def prefix(kv_pages, prefix_table, prefix_lens, first_seq) -> kvsel_prefix:
     if prefix_table.dim() != 2 or prefix_lens.numel() != prefix_table.shape[0] \
             or first_seq.numel() != prefix_table.shape[0] + 1:
         raise ValueError("prefix: expected prefix_table [n, blocks], prefix_lens [n] and first_seq [n + 1]")
-    return kvsel_prefix(prefix_table.shape[0], prefix_table.shape[1], _ptr(kv_pages), kv_pages.shape[0],
-                        _ptr(prefix_table), _ptr(prefix_lens), _ptr(first_seq))
+    return _placed(kvsel_prefix(prefix_table.shape[0], prefix_table.shape[1], _ptr(kv_pages), kv_pages.shape[0],
+                                _ptr(prefix_table), _ptr(prefix_lens), _ptr(first_seq)),
+                   kv_pages, prefix_table, prefix_lens, first_seq)
 
 
 def kvsel_prefix_decode(p, px: kvsel_prefix, q, out, lse, ws, softmax_scale, own_out=None, own_lse=None,
@@ -585,7 +599,7 @@ def kvsel_prefix_decode(p, px: kvsel_prefix, q, out, lse, ws, softmax_scale, own
         _expect(t, dt, n)
         if t is not None and t.numel() != size:
             raise ValueError(f"{n}: expected {size} elements, got {t.numel()}")
-    _here(q, out, lse, own_out, own_lse, out_bf16, ws)
+    _here(q, out, lse, own_out, own_lse, out_bf16, ws, desc=px)
     _check(lib().kvsel_prefix_decode(ctypes.byref(p), ctypes.byref(px), _ptr(q), float(softmax_scale), _ptr(own_out),
                                      _ptr(own_lse), _ptr(out), _ptr(out_bf16), _ptr(lse), _ptr(ws),
                                      ws.numel() * ws.element_size(), _stream(stream)),
@@ -631,6 +645,8 @@ def kvsel_sparse_decode(p, q, kv: kvsel_kv_src, seq_lens, sel_idx, n_sel, out, l
                      (out, torch.float32, "out"), (lse, torch.float32, "lse"),
                      (dense_flag, torch.uint8, "dense_flag"), (out_bf16, torch.bfloat16, "out_bf16")):
         _expect(t, dt, n)
+    if hasattr(kv, "device"):                      # 8-bit pages
+        _here(q, desc=kv)
     _check(lib().kvsel_sparse_decode(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(seq_lens),
                                      _ptr(sel_idx), _ptr(n_sel), _ptr(span_start), _ptr(span_len),
                                      _ptr(n_spans), _ptr(dense_flag), float(softmax_scale),
