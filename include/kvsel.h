@@ -408,7 +408,8 @@ typedef struct kvsel_kv_src {
  * with, and below that is off by at most 2^-40 of the largest. A row that was not
  * finite when it was written makes the outputs that attend it NaN.
  * out: device fp32 output; out_bf16: optional bf16 copy; lse: device fp32.
- * ws: kvsel_workspace_size(p, KVSEL_WS_SPARSE_DECODE) bytes (no initial
+ * ws: kvsel_workspace_size(p, KVSEL_WS_SPARSE_DECODE) bytes, enough for every
+ * kind, or KVSEL_WS_SPARSE_DECODE_BF16 for the kinds of bf16 data (no initial
  * contents required). Two kernels: the attention grid and a row merge grid
  * launched as its programmatic dependent.
  * Errors: UNSUPPORTED when batch * n_kvheads * max_blocks >= 2^31 (the tile
@@ -680,7 +681,8 @@ enum kvsel_ws_kind {
   KVSEL_WS_SCORE_TOPK = 0,
   KVSEL_WS_SPARSE_DECODE = 1,
   KVSEL_WS_CACHE_FETCH = 2,
-  KVSEL_WS_PREFIX_DECODE = 3
+  KVSEL_WS_PREFIX_DECODE = 3,
+  KVSEL_WS_SPARSE_DECODE_BF16 = 4 /* kvsel_sparse_decode on any kind but the 8-bit pages */
 };
 
 /* Workspace bytes an entry point needs for problem p (0 on bad input). */

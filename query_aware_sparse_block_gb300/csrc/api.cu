@@ -1,6 +1,7 @@
 // C ABI of libkvsel: argument checks, workspace sizing, the host-side budget
 // model and the per-device error word. Kernels live in summaries.cu,
 // score_topk.cu, sparse_decode.cuh, q8_cache.cu, prefix_decode.cu and offload.cu.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -170,7 +171,8 @@ int64_t kvsel_kv_bytes_per_token(int32_t layers, int32_t kv_heads, int32_t head_
 size_t kvsel_workspace_size(const kvsel_problem* p, int which) {
   if (check_problem(p) != KVSEL_OK) return 0;
   if (which == KVSEL_WS_SCORE_TOPK) return score_topk_ws_bytes(*p);
-  if (which == KVSEL_WS_SPARSE_DECODE) return sparse_decode_ws_bytes(*p);
+  if (which == KVSEL_WS_SPARSE_DECODE) return std::max(sparse_decode_ws_bytes(*p, false), sparse_decode_ws_bytes(*p, true));
+  if (which == KVSEL_WS_SPARSE_DECODE_BF16) return sparse_decode_ws_bytes(*p, false);
   if (which == KVSEL_WS_CACHE_FETCH) return cache_fetch_ws_bytes(*p);
   if (which == KVSEL_WS_PREFIX_DECODE) return prefix_decode_ws_bytes(*p);
   return 0;
@@ -767,13 +769,14 @@ int kvsel_sparse_decode(const kvsel_problem* p, const kvsel_bf16* q, const kvsel
   // the tile list is counted in int32 (every block of every sequence, dense, per KV head)
   if (int64_t(p->batch) * p->n_kvheads * p->max_blocks >= (int64_t(1) << 31))
     return fail(KVSEL_ERR_UNSUPPORTED, "sparse_decode: batch * n_kvheads * max_blocks must be below 2^31");
-  if (!ws || ws_bytes < sparse_decode_ws_bytes(*p) || !aligned16(ws))
+  const bool q8 = kv->kind == KVSEL_KV_PAGED_E4M3 || kv->kind == KVSEL_KV_PAGED_INT8;
+  if (!ws || ws_bytes < sparse_decode_ws_bytes(*p, q8) || !aligned16(ws))
     return fail(KVSEL_ERR_WORKSPACE, "sparse_decode: workspace missing, small or misaligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* ew = device_error_word();
   if (!ew) return fail(KVSEL_ERR_CUDA, "sparse_decode: no CUDA device");
   kvsel_kv_src src = *kv;
-  if (kv->kind == KVSEL_KV_PAGED || kv->kind == KVSEL_KV_PAGED_E4M3 || kv->kind == KVSEL_KV_PAGED_INT8) {
+  if (kv->kind == KVSEL_KV_PAGED || q8) {
     if (!kv->kv_pages || !kv->block_table || kv->n_pages <= 0)
       return fail(KVSEL_ERR_INVALID_ARG, "sparse_decode: paged source needs pages and a block table");
     if (!aligned16(kv->kv_pages))

@@ -72,7 +72,7 @@ cudaError_t launch_merge_spans(const kvsel_problem& p, const int32_t* sel_idx,
                                int32_t* n_spans, int* err, cudaStream_t s);
 
 // ---- sparse decode (sparse_decode.cu) ----
-size_t sparse_decode_ws_bytes(const kvsel_problem& p);
+size_t sparse_decode_ws_bytes(const kvsel_problem& p, bool q8);   // for 8-bit pages, or for bf16 data
 cudaError_t launch_sparse_decode(const kvsel_problem& p, const kvsel_bf16* q,
                                  const kvsel_kv_src& kv, const int32_t* seq_lens,
                                  const int32_t* sel_idx, const int32_t* n_sel,

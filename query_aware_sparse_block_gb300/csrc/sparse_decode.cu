@@ -8,18 +8,19 @@ cudaError_t launch_decode_bf16(const kvsel_problem& p, const DecodeArgs& a, cuda
   return launch_shape<kFmtBf16>(p, a, s);
 }
 
-// (sequence, head group) segments of the format that has the most: pairs of
-// 16-token blocks leave room for half as many heads in a tile.
-static size_t segments_of(const kvsel_problem& p) {
-  return size_t(p.batch) * (p.n_kvheads / heads_per_group(p.block_size == 16 ? 32 : p.block_size, p.n_kvheads));
+// (sequence, head group) segments: 8-bit blocks of 16 tokens come in pairs, which
+// leaves room for half as many heads in a tile.
+static size_t segments_of(const kvsel_problem& p, bool q8) {
+  const int tokens = q8 && p.block_size == 16 ? 32 : p.block_size;
+  return size_t(p.batch) * (p.n_kvheads / heads_per_group(tokens, p.n_kvheads));
 }
 
-size_t decode_meta_bytes(const kvsel_problem& p) { return (segments_of(p) * 8 + 255) / 256 * 256; }
+static size_t decode_meta_bytes(const kvsel_problem& p, bool q8) { return (segments_of(p, q8) * 8 + 255) / 256 * 256; }
 
-size_t sparse_decode_ws_bytes(const kvsel_problem& p) {
+size_t sparse_decode_ws_bytes(const kvsel_problem& p, bool q8) {
   const int G = p.n_qheads / std::max(1, p.n_kvheads);
-  const size_t parts = (size_t(kMaxCtas) + segments_of(p)) * kMaxWarps * G * (p.head_dim + 4) * 4;
-  return decode_meta_bytes(p) + parts;
+  const int warps = q8 ? decode_warps<kFmtE4M3>(p.head_dim, G) : decode_warps<kFmtBf16>(p.head_dim, G);
+  return decode_meta_bytes(p, q8) + (size_t(kMaxCtas) + segments_of(p, q8)) * warps * G * (p.head_dim + 4) * 4;
 }
 
 cudaError_t launch_sparse_decode(const kvsel_problem& p, const kvsel_bf16* q,
@@ -41,7 +42,7 @@ cudaError_t launch_sparse_decode(const kvsel_problem& p, const kvsel_bf16* q,
   a.out = out; a.out_bf16 = out_bf16; a.lse = lse;
   char* w = static_cast<char*>(ws);
   a.seg_info = reinterpret_cast<int2*>(w);
-  a.partials = reinterpret_cast<float*>(w + decode_meta_bytes(p));
+  a.partials = reinterpret_cast<float*>(w + decode_meta_bytes(p, q8));
   a.err = err;
   a.batch = p.batch; a.Hq = p.n_qheads; a.Hkv = p.n_kvheads; a.G = p.n_qheads / p.n_kvheads;
   a.B = p.block_size; a.max_blocks = p.max_blocks; a.k_max = p.k_max;

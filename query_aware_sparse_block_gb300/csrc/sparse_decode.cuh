@@ -118,7 +118,6 @@ enum DecodeFormat { kFmtBf16 = 0, kFmtE4M3 = 1, kFmtInt8 = 2 };
 
 constexpr int kTileRows = 64;          // token rows of a tile (of all its heads)
 constexpr int kMaxCtas = 256;          // partial-slot capacity of the workspace
-constexpr int kMaxWarps = 16;          // of a CTA
 constexpr int kDenseSeq = 1 << 30;     // flag beside a sequence's length (at most 2^20)
 // Flags beside a segment's CTA count: a CTA whose range lies in one segment has joined
 // its warps' states (8-bit pages). Every CTA between a segment's first and last does.
@@ -142,6 +141,21 @@ inline int heads_per_group(int B, int Hkv) {
   int h = std::min(Hkv, kTileRows / B);
   while (h > 1 && Hkv % h) --h;
   return std::max(1, h);
+}
+
+// Rings of a CTA and 16-token subtiles of a warp (launch_group), and the warps that
+// they make: the states' slots of a CTA and segment.
+template <int FMT>
+constexpr int decode_rings(int D, int G) {
+  return FMT == kFmtBf16 ? 2 : D == 128 && G > 8 ? 4 : 6;
+}
+template <int FMT>
+constexpr int decode_subtiles() {
+  return FMT == kFmtBf16 ? 1 : 2;
+}
+template <int FMT>
+constexpr int decode_warps(int D, int G) {
+  return decode_rings<FMT>(D, G) * (4 / decode_subtiles<FMT>());
 }
 
 // Bytes of the K and V of HPG heads of one block, the unit of a copy.
@@ -1214,9 +1228,7 @@ cudaError_t launch_t(const kvsel_problem& p, const DecodeArgs& a0, cudaStream_t 
 // thread.
 template <int D, int B, int NTH, int FMT>
 cudaError_t launch_group(const kvsel_problem& p, const DecodeArgs& a, cudaStream_t s) {
-  constexpr bool kWide = D == 128 && NTH == 2;
-  if constexpr (FMT == kFmtBf16) return launch_t<D, B, NTH, FMT, 2, 1>(p, a, s);
-  else return launch_t<D, B, NTH, FMT, kWide ? 4 : 6, 2>(p, a, s);
+  return launch_t<D, B, NTH, FMT, decode_rings<FMT>(D, 8 * NTH), decode_subtiles<FMT>()>(p, a, s);
 }
 
 template <int D, int B, int FMT>

@@ -36,6 +36,7 @@ KVSEL_WS_SCORE_TOPK = 0
 KVSEL_WS_SPARSE_DECODE = 1
 KVSEL_WS_CACHE_FETCH = 2
 KVSEL_WS_PREFIX_DECODE = 3
+KVSEL_WS_SPARSE_DECODE_BF16 = 4
 KVSEL_SCORE_PATH_AUTO = 0
 KVSEL_SCORE_PATH_TWO_GRID = 1
 KVSEL_SCORE_PATH_CLUSTER = 2

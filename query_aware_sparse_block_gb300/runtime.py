@@ -31,13 +31,14 @@ class SparseDecoder:
         self.dense_flag = torch.zeros((b,), dtype=torch.uint8, device=self.device)
         self.k_per_seq = torch.zeros((b,), **i32)
         ws1 = K.kvsel_workspace_size(self.p, K.KVSEL_WS_SCORE_TOPK)
-        ws2 = K.kvsel_workspace_size(self.p, K.KVSEL_WS_SPARSE_DECODE)
+        ws2 = K.kvsel_workspace_size(self.p, K.KVSEL_WS_SPARSE_DECODE_BF16)
         if ws1 == 0 or ws2 == 0:
             raise K.KvselError(K.KVSEL_ERR_UNSUPPORTED, "SparseDecoder",
                                K.lib().kvsel_last_error().decode())
         # no workspace needs initial contents; zero-filled only for tidiness
         self.ws_score = torch.zeros((ws1,), dtype=torch.uint8, device=self.device)
         self.ws_decode = torch.zeros((ws2,), dtype=torch.uint8, device=self.device)
+        self.ws_decode_q8 = None               # 8-bit pages need more: reserve_q8()
         self.out = torch.zeros((b, n_qheads, head_dim), dtype=torch.float32, device=self.device)
         self.lse = torch.zeros((b, n_qheads), dtype=torch.float32, device=self.device)
         # the kernels take fp32; keep the exact value they see
@@ -89,11 +90,22 @@ class SparseDecoder:
                                   self.ws_score, app=app, gamma=gamma, tau_rel=tau_rel,
                                   dense_flag=self.dense_flag, scores_out=scores_out, stream=stream)
 
+    def reserve_q8(self):
+        """The workspace of the attention on 8-bit pages. A Q8Cache reserves it, so that no
+        attend() of its pages allocates."""
+        if self.ws_decode_q8 is None:
+            n = K.kvsel_workspace_size(self.p, K.KVSEL_WS_SPARSE_DECODE)
+            self.ws_decode_q8 = torch.empty((n,), dtype=torch.uint8, device=self.device)
+        return self.ws_decode_q8
+
+    def decode_workspace(self, kv):
+        return self.reserve_q8() if kv.kind in (K.KVSEL_KV_PAGED_E4M3, K.KVSEL_KV_PAGED_INT8) else self.ws_decode
+
     def attend(self, q, kv, seq_lens, use_dense_flag=True, out=None, lse=None, out_bf16=None,
                stream=None):
         K.kvsel_sparse_decode(self.p, q, kv, seq_lens, self.sel_idx, self.n_sel,
                               self.out if out is None else out, self.lse if lse is None else lse,
-                              self.ws_decode, self.scale,
+                              self.decode_workspace(kv), self.scale,
                               dense_flag=self.dense_flag if use_dense_flag else None,
                               span_start=self.span_start, span_len=self.span_len,
                               n_spans=self.n_spans, out_bf16=out_bf16, stream=stream)
@@ -157,7 +169,8 @@ class BoundLayer:
                     vp(d.span_len.data_ptr()), vp(d.n_spans.data_ptr()), vp(d.dense_flag.data_ptr()))
         self.kps = vp(d.k_per_seq.data_ptr())
         self.ws1, self.ws1n = vp(d.ws_score.data_ptr()), ctypes.c_size_t(d.ws_score.numel())
-        self.ws2, self.ws2n = vp(d.ws_decode.data_ptr()), ctypes.c_size_t(d.ws_decode.numel())
+        ws2 = d.decode_workspace(self.kv)
+        self.ws2, self.ws2n = vp(ws2.data_ptr()), ctypes.c_size_t(ws2.numel())
         self.scale = ctypes.c_float(d.scale)
         self._app = K.kvsel_append_in()
         self._app.kv_pages, self._app.n_pages = self.kv_pages.value, self.n_pages
@@ -265,6 +278,7 @@ class Q8Cache:
         self.pages, self.block_table = pages, block_table
         self.desc = K.q8_cache(self.FORMATS[fmt], pages, block_table)
         self.kv = K.kv_paged_q8(self.desc)
+        dec.reserve_q8()
 
     def write(self, row_start, start_pos, k, v, summaries=None, stream=None):
         """Quantise ragged rows into the pages and update the summaries of
