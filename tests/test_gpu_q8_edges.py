@@ -184,3 +184,50 @@ def test_bound_layer_appends_rows_of_a_projection(K):
         layer.append(ptr(pos), s, None if given is None else ptr(given))
         torch.cuda.synchronize()
         assert (cache.pages != 0).any() and torch.equal(cache.pages, want.pages) and torch.equal(summ, ws)
+
+
+@pytest.mark.parametrize("fmt,batch,hq,hkv,d,B,most", [("e4m3", 25, 32, 32, 128, 64, 10), ("int8", 3, 8, 8, 128, 64, 600),
+                                                       ("int8", 61, 28, 4, 64, 16, 40), ("e4m3", 5, 32, 2, 128, 32, 500)])
+def test_ragged_decode_over_the_whole_grid(K, fmt, batch, hq, hkv, d, B, most):
+    """Segments of unequal length over every CTA: CTAs of one segment, which join their states, CTAs of several, rings
+    that pass over a segment without a tile of theirs, some sequences empty. The pages are random codes."""
+    from query_aware_sparse_block_gb300.runtime import Q8Cache, SparseDecoder
+    g = torch.Generator().manual_seed(batch + most)
+    lens = torch.randint(0, most * B + 1, (batch,), generator=g)
+    lens[0], lens[-1] = most * B, 0
+    mb = most + 1
+    dec = SparseDecoder(batch, hq, hkv, d, B, mb, device="cuda:0")
+    table = torch.randperm(batch * mb, generator=g).view(batch, mb)
+    cache = Q8Cache(dec, fmt, table.to(torch.int32).cuda(), n_pages=batch * mb)
+    codes, byte = cache.pages[..., :2 * B * d], cache.pages[..., 2 * B * d:]
+    c = torch.randint(0, 256, codes.shape, generator=g, dtype=torch.uint8)
+    if fmt == "e4m3":
+        c[(c & 127) > 0x70] = 0x30                                        # up to 128; no NaN
+    codes.copy_(c)
+    byte.copy_(torch.randint(118, 122, byte.shape, generator=g, dtype=torch.uint8))
+    q = torch.randn((batch, hq, d), generator=g).to(torch.bfloat16).cuda()
+    dec.dense_flag.fill_(1)
+    dec.attend(q, cache.kv, lens.to(torch.int32).cuda())
+    torch.cuda.synchronize()
+    values = torch.from_numpy(_q8.code_values(fmt)).cuda()
+    at = torch.from_numpy(_q8.chunk_index(B, d)).cuda()
+    G = hq // hkv
+    for b, T in enumerate(lens.tolist()):
+        if T == 0:
+            assert (dec.out[b] == 0).all() and (dec.lse[b] == -float("inf")).all()
+            continue
+        raw = cache.pages[table[b, :-(-T // B)].cuda()]
+        kv = []
+        for w in (0, 1):
+            x = values[raw[..., w * B * d:(w + 1) * B * d].long()][..., at]           # [n][H][B][d]
+            f = 2.0 ** (raw[..., 2 * B * d + w * B:2 * B * d + (w + 1) * B].double() - 127)
+            kv.append((x * f[..., None]).transpose(0, 1).reshape(hkv, -1, d)[:, :T])
+        k, v = kv
+        qd = q[b].double().view(hkv, G, d)
+        s = qd @ k.transpose(-1, -2) * dec.scale
+        z = torch.logsumexp(s, -1)
+        ref = torch.exp(s - z[..., None]) @ v
+        reach = (qd.abs() @ k.abs().transpose(-1, -2) * dec.scale).amax(-1)
+        t_out, t_lse = _q8.tolerances(reach, T, v.abs().amax((1, 2))[:, None], d)
+        assert ((dec.out[b].double().view(hkv, G, d) - ref).abs().amax(-1) <= t_out).all(), b
+        assert ((dec.lse[b].double().view(hkv, G) - z).abs() <= t_lse + 2.0 ** -23 * z.abs()).all(), b
