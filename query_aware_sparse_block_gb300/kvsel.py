@@ -533,8 +533,14 @@ def _here(*tensors, desc=None):
             if not t.is_cuda:
                 raise TypeError("expected CUDA tensors")
             raise ValueError(f"expected tensors on the current device, cuda:{device}, got one on {t.device}")
-    if getattr(desc, "device", device) != device:
-        raise ValueError(f"expected pages and tables on the current device, cuda:{device}, they are on cuda:{desc.device}")
+    if desc is not None:
+        _pages_here(desc, device)
+
+
+def _pages_here(desc, device=None):
+    at = getattr(desc, "device", None)
+    if at is not None and at != (torch.cuda.current_device() if device is None else device):
+        raise ValueError(f"expected pages and tables on the current device, they are on cuda:{at}")
 
 
 def _ragged(p, row_start, start_pos):
@@ -646,8 +652,7 @@ def kvsel_sparse_decode(p, q, kv: kvsel_kv_src, seq_lens, sel_idx, n_sel, out, l
                      (out, torch.float32, "out"), (lse, torch.float32, "lse"),
                      (dense_flag, torch.uint8, "dense_flag"), (out_bf16, torch.bfloat16, "out_bf16")):
         _expect(t, dt, n)
-    if hasattr(kv, "device"):                      # 8-bit pages
-        _here(q, desc=kv)
+    _pages_here(kv)
     _check(lib().kvsel_sparse_decode(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(seq_lens),
                                      _ptr(sel_idx), _ptr(n_sel), _ptr(span_start), _ptr(span_len),
                                      _ptr(n_spans), _ptr(dense_flag), float(softmax_scale),

@@ -99,7 +99,7 @@ class SparseDecoder:
         return self.ws_decode_q8
 
     def decode_workspace(self, kv):
-        return self.reserve_q8() if kv.kind in (K.KVSEL_KV_PAGED_E4M3, K.KVSEL_KV_PAGED_INT8) else self.ws_decode
+        return self.ws_decode if kv.kind < K.KVSEL_KV_PAGED_E4M3 else self.reserve_q8()
 
     def attend(self, q, kv, seq_lens, use_dense_flag=True, out=None, lse=None, out_bf16=None,
                stream=None):
