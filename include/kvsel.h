@@ -413,7 +413,8 @@ typedef struct kvsel_kv_src {
  * contents required). Two kernels: the attention grid and a row merge grid
  * launched as its programmatic dependent.
  * Errors: UNSUPPORTED when batch * n_kvheads * max_blocks >= 2^31 (the tile
- * list is counted in int32).
+ * list is counted in int32), or n_pages * n_kvheads * 2 * block_size >= 2^31
+ * (bf16 pages), n_pages * n_kvheads >= 2^31 (8-bit pages).
  */
 KVSEL_API int kvsel_sparse_decode(const kvsel_problem* p, const kvsel_bf16* q, const kvsel_kv_src* kv,
                         const int32_t* seq_lens, const int32_t* sel_idx, const int32_t* n_sel,

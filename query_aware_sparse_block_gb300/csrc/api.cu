@@ -781,8 +781,11 @@ int kvsel_sparse_decode(const kvsel_problem* p, const kvsel_bf16* q, const kvsel
       return fail(KVSEL_ERR_INVALID_ARG, "sparse_decode: paged source needs pages and a block table");
     if (!aligned16(kv->kv_pages))
       return fail(KVSEL_ERR_INVALID_ARG, "sparse_decode: misaligned pages");
-    if (kv->n_pages * p->n_kvheads * 2 * p->block_size >= (int64_t(1) << 31))
-      return fail(KVSEL_ERR_UNSUPPORTED, "sparse_decode: more than 2^31 cache rows");
+    // bf16 rows, and the heads of 8-bit pages, are counted in int32 (2^31 rows of 65 bytes are 140 GB,
+    // which the device holds)
+    const int64_t per_page = int64_t(p->n_kvheads) * (q8 ? 1 : 2 * p->block_size);
+    if (kv->n_pages > ((int64_t(1) << 31) - 1) / per_page)
+      return fail(KVSEL_ERR_UNSUPPORTED, "sparse_decode: too many pages (2^31 bf16 rows, or heads of 8-bit pages)");
   } else if (kv->kind == KVSEL_KV_STAGED || kv->kind == KVSEL_KV_HOST) {
     if (kv->kind == KVSEL_KV_HOST) {
       if (!span_start || !span_len || !n_spans)

@@ -231,3 +231,26 @@ def test_ragged_decode_over_the_whole_grid(K, fmt, batch, hq, hkv, d, B, most):
         t_out, t_lse = _q8.tolerances(reach, T, v.abs().amax((1, 2))[:, None], d)
         assert ((dec.out[b].double().view(hkv, G, d) - ref).abs().amax(-1) <= t_out).all(), b
         assert ((dec.lse[b].double().view(hkv, G) - z).abs() <= t_lse + 2.0 ** -23 * z.abs()).all(), b
+
+
+def test_a_cache_of_more_rows_than_int32_counts_is_attended(K):
+    """A pool of 2^31 rows and more (140 GB at d = 64): the descriptor names that many pages, the table only the first."""
+    from query_aware_sparse_block_gb300.runtime import Q8Cache, SparseDecoder
+    H, d, B, mb = 2, 64, 16, 4
+    dec = SparseDecoder(1, H, H, d, B, mb, device="cuda:0")
+    cache = Q8Cache(dec, "int8", torch.arange(mb, dtype=torch.int32).view(1, mb).cuda(), n_pages=mb)
+    g = torch.Generator().manual_seed(2)
+    k, v = (_q8.rows(g, (60, H, d)).cuda() for _ in range(2))
+    cache.write(_i32([0, 60]), _i32([0]), k, v)
+    q = torch.randn((1, H, d), generator=g).to(torch.bfloat16).cuda()
+    dec.n_sel[0], dec.sel_idx[0] = mb, torch.arange(mb, dtype=torch.int32)
+    dec.attend(q, cache.kv, _i32([60]))
+    want = dec.out.clone()
+    cache.kv.n_pages = (1 << 31) // (H * 2 * B) + 1
+    dec.attend(q, cache.kv, _i32([60]))
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all() and torch.equal(dec.out, want)
+    cache.kv.n_pages = (1 << 31) // H
+    with pytest.raises(K.KvselError) as e:
+        dec.attend(q, cache.kv, _i32([60]))
+    assert e.value.code == K.KVSEL_ERR_UNSUPPORTED
