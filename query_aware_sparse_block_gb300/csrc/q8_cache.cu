@@ -133,7 +133,9 @@ __device__ __forceinline__ void store_row16(kvsel_bf16* p, const Row16& r, bool 
 
 // 16 stored codes times their factor added to the block's column sums, in
 // units of 2^8 (64 rows of the largest value stay in range). The product is
-// exact, the sum rounds once a row.
+// exact, the sum rounds once a row: a pair of fp32 sums that carries each
+// addition's error (about 48 bits) took 92.1 us for the large write's 70.5 and 4.27
+// for a decode step's 3.82.
 template <int FMT>
 __device__ __forceinline__ void add_key(float2 (&s)[8], uint4 codes, uint32_t byte) {
   const float f1 = q8_factor(byte) * 0x1p-8f;

@@ -293,7 +293,8 @@ class Q8Cache:
 class SharedPrefix:
     """Prefixes that consecutive sequences of the batch share, in bf16 pages
     (kvsel_prefix_decode): attend() reads each prefix once for all its
-    sequences and joins the result with their own attention."""
+    sequences and joins the result with their own attention. The call plans by
+    prefix_table's width: make it as wide as the prefixes are long."""
 
     def __init__(self, dec: SparseDecoder, kv_pages, prefix_table, prefix_lens, first_seq):
         p = self.p = dec.p
