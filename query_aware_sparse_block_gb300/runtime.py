@@ -179,11 +179,14 @@ class BoundLayer:
         self._app_ref = ctypes.byref(self._app)
 
     def _stride(self, rows, name):
-        if rows is None:
-            return self.dec.p.n_kvheads * self.dec.p.head_dim
-        n, stride = K._rows(rows, self.dec.p, name)
-        if n != self.dec.p.batch:
-            raise ValueError(f"{name}: expected a row for each of {self.dec.p.batch} sequences, got {n}")
+        p = self.dec.p
+        n, stride = p.batch, p.n_kvheads * p.head_dim
+        if rows is not None and rows.dtype == torch.bfloat16 and rows.is_contiguous():
+            n = rows.numel() // stride                           # of whatever shape
+        elif rows is not None:
+            n, stride = K._rows(rows, p, name)
+        if n < p.batch:
+            raise ValueError(f"{name}: expected a row for each of {p.batch} sequences, got {n}")
         return stride
 
     def append(self, append_pos_ptr, stream_ptr, new_k_ptr=None, new_v_ptr=None):

@@ -31,12 +31,16 @@ def test_rows_of_a_projection_keep_their_strides(K):
     assert (layer.k_stride, layer.v_stride) == (512, 128)
     layer = _layer(K)
     assert (layer.k_stride, layer.v_stride) == (128, 128)
+    layer = _layer(K, new_k=torch.zeros((3, 128), dtype=torch.bfloat16), new_v=torch.zeros((5, 2, 64), dtype=torch.bfloat16))
+    assert (layer.k_stride, layer.v_stride) == (128, 128)                # contiguous rows of any shape, and more of them
+    layer = _layer(K, new_k=torch.zeros((5, 8, 64), dtype=torch.bfloat16)[:, :2])
+    assert layer.k_stride == 512
 
 
 @pytest.mark.parametrize("bad,error", [
     (torch.zeros((3, 2, 64)), TypeError),
     (torch.zeros((2, 2, 64), dtype=torch.bfloat16), ValueError),
-    (torch.zeros((3, 128), dtype=torch.bfloat16), ValueError),
+    (torch.zeros((3, 256), dtype=torch.bfloat16)[:, :128], ValueError),
     (torch.zeros((3, 2, 128), dtype=torch.bfloat16)[..., ::2], ValueError),
     (torch.zeros((2, 3, 64), dtype=torch.bfloat16).transpose(0, 1), ValueError),
 ], ids=["fp32", "two rows", "flat", "every second channel", "heads apart"])
